@@ -1,7 +1,7 @@
 // mla_noalloc.cu — paged MLA decode for callers that cannot allocate device
 // memory.
 //
-// mla_decode_paged and mla_combine_splits need scratch memory from the
+// mla_decode_paged and its merge need scratch memory from the
 // caller: a workspace (the split plan and a status word) and the per-split
 // partial outputs.  Some callers have no way to provide it: an inference
 // engine whose memory planner hands out every byte of the GPU before the
@@ -106,8 +106,11 @@ extern "C" int mla_decode_attend_noalloc(const mla_dims* d, const void* q_cat, c
   if ((rc = mla_decode_paged(d, q_cat, kv_cache, block_table, seq_lens, 0, o_part, lse_part, ws,
                              ws_bytes, stream)) != MLA_OK)
     return rc;
-  if ((rc = mla_combine_splits(d, o_part, lse_part, ws, ws_bytes, o_lat, lse, stream)) != MLA_OK)
-    return rc;
+  // merged with the slots that the scratch holds as the bound: a plan spoilt by
+  // another call on the array (see above) must not lead past its end
+  if (launch_combine(o_part, lse_part, static_cast<const WsHeader*>(ws), o_lat, lse, d->B, d->Lq, d->H, d->G, slots,
+                     st) != cudaSuccess)
+    return MLA_ERR_CUDA;
   if (device_status &&
       cudaMemcpyAsync(device_status, ws, sizeof(int), cudaMemcpyDeviceToDevice, st) != cudaSuccess)
     return MLA_ERR_CUDA;
