@@ -430,6 +430,7 @@ int mla_prefill_attend(const mla_dims* dims, const void* q_nope, const void* q_r
  *             cached place s of sequence b; the caller zero-fills it when the
  *             sequence begins, mla_cache_evict leaves zeros behind the end
  *   position  int32 [B, max_pages_per_seq * 64]: its position in the text
+ *             (mla_cache_append with start_position; see there)
  *   workspace / ws_bytes: at least 32 bytes whose first int is the sticky
  *             status word, zeroed once (mla_cache_evict needs more)
  */
@@ -449,7 +450,11 @@ int mla_prefill_attend(const mla_dims* dims, const void* q_nope, const void* q_r
  * both rounded to nearest, ties to even.  A block that holds an infinity or a
  * NaN reads back as NaN and sets MLA_ERR_RANGE.
  * position (may be NULL): receives start_position[b] + l of each written
- *   token (start_position int32 [B]; NULL: its cached place).
+ *   token (start_position int32 [B]; NULL: its cached place, which is its
+ *   text position only while nothing of the sequence has been evicted: an
+ *   eviction cuts seq_lens, not the text, and mla_cache_evict would take
+ *   every later token for equally new.  A loop that evicts counts the text
+ *   itself and passes it).
  * c_cached bf16 [B,Lq,d_c] (may be NULL): receives the latent as the cache
  *   now holds it (exact in bf16), for callers whose own attention over the
  *   new tokens shall see what later steps will read.  Padding rows are left.

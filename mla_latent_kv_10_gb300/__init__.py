@@ -352,7 +352,10 @@ KV_BF16, KV_FP8, KV_FP4 = 0, 1, 2  # mirror of mla_kv_format
 def mla_cache_append(dims, kv_format, c_kv, k_rope, block_table, seq_lens, kv_cache, workspace, n_new=None,
                      start_position=None, position=None, c_cached=None, stream=None):
     """Write the new tokens' latents and RoPE keys into the paged cache in its
-    format (KV_BF16, KV_FP8 or KV_FP4); seq_lens count the new tokens."""
+    format (KV_BF16, KV_FP8 or KV_FP4); seq_lens count the new tokens.
+    position records start_position[b] + l, the text positions that
+    mla_cache_evict goes by (without start_position the cached places, which
+    are the text positions only until a sequence is first cut)."""
     _check(load_library().mla_cache_append(
         _dims(dims), int(kv_format), _ptr(c_kv), _ptr(k_rope), _ptr(block_table), _ptr(seq_lens), _ptr(n_new),
         _ptr(start_position), _ptr(kv_cache), _ptr(position), _ptr(c_cached), _ptr(workspace),
