@@ -481,7 +481,9 @@ int mla_cache_append(const mla_dims* dims, int kv_format, const void* c_kv,
  * kv_cache (in kv_format), block_table and seq_lens as for the decode; rows
  * past a sequence's end are not used.  Errors as for mla_decode_paged
  * (workspace: 32 bytes), and MLA_ERR_RANGE (device) for FP8 and FP4 caches as
- * in their decodes.
+ * in their decodes.  The weights of a sequence with a bad length (an idle
+ * place of the batch with seq_lens[b] = 0, say) and those of tokens behind a
+ * bad table entry are left as they were.
  */
 int mla_cache_weights(const mla_dims* dims, int kv_format, const void* q_cat,
                       const void* kv_cache, const int32_t* block_table,

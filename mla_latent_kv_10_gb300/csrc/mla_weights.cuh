@@ -464,6 +464,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     uint32_t t = 0;
     while (next_range()) {
       const int n = walk.len(a, sb);
+      // `weight` outlives the call: nothing is added to a sequence whose length
+      // was clamped, nor to tokens behind a table entry that was replaced
+      const bool whole = a.seq_lens[sb] == n;
       for (int pass = 0; pass < passes; ++pass) {
         const int g = pass / blocks, r0 = (pass % blocks) * N;
         bar_sync(1, 32 * kSumWarps);  // the pass before has read its rows
@@ -489,6 +492,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         bar_sync(1, 32 * kSumWarps);
         for (int i = ta; i < tb; ++i, ++t) {
+          const int at = i * kWTok + r;  // requested ahead of the wait
+          const int page = whole && at < n ? a.block_table[(size_t)sb * a.max_pages + at / kPage] : -1;
           if (ok) ok = wait(sh.s_full[t & 1], t >> 1);
           if (!ok) continue;  // (the barriers above still see every warp)
           tc_fence_after();
@@ -526,10 +531,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(sh.s_free[t & 1]));
-          if (i * kWTok + r < n) {
-            float* at = weight + (size_t)sb * a.max_pages * kPage + (size_t)i * kWTok + r;
-            *at += sum;
-          }
+          if (page >= 0 && page < a.num_pages) weight[(size_t)sb * a.max_pages * kPage + at] += sum;
         }
       }
     }
