@@ -516,7 +516,9 @@ int mla_cache_evict_workspace_size(const mla_dims* dims, size_t* bytes);
  * MLA_ERR_INVALID_ARG (null, unknown format, budget < 1, recent or first < 0,
  * recent + first > budget) / UNSUPPORTED / MISALIGNED / WORKSPACE / CUDA;
  * device: MLA_ERR_BAD_SEQLEN (the sequence is left alone), MLA_ERR_BAD_TABLE
- * (a row behind a bad entry is not moved).
+ * (where the entry of a moving token or of its place is bad, nothing moves:
+ * the place keeps the token that was to be evicted, row, weight and position,
+ * and the other one is lost with the tokens behind the new end).
  */
 int mla_cache_evict(const mla_dims* dims, int kv_format, int budget, int recent,
                     int first, const int32_t* block_table, void* kv_cache,

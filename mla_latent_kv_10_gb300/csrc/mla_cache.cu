@@ -515,15 +515,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_kernel(const EvictArgs a)
       const int pt = table[to / kPage], pf = table[from / kPage];
       const float w = weight[from];
       const int p = position[from];
-      if (pt < 0 || pt >= a.num_pages || pf < 0 || pf >= a.num_pages) {  // never dereferenced
+      if (pt < 0 || pt >= a.num_pages || pf < 0 || pf >= a.num_pages) {
+        // never dereferenced; the place keeps its row, and what is said of it
         set_status(a.ws, MLA_ERR_BAD_TABLE);
       } else {
         src = ((long long)pf * kPage + from % kPage) * chunks;
         dst = ((long long)pt * kPage + to % kPage) * chunks;
+        weight[to] = w;
+        position[to] = p;
       }
-      weight[to] = w;
       weight[from] = 0.f;
-      position[to] = p;
     }
     uint4* rows = reinterpret_cast<uint4*>(a.cache);
     for (uint32_t q0 = 0; q0 < cnt; q0 += kMoveRows) {

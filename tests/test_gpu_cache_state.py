@@ -1,11 +1,13 @@
 """GPU tests of what mla_cache_weights and mla_cache_evict leave behind: the
 weights and positions outlive the call, so a sequence or a page that the call
 refuses must not change them."""
+import numpy as np
 import pytest
 import torch
 
 import mla_latent_kv_10_gb300 as mla
-from test_gpu_cache import FMT, MLA_ERR_BAD_SEQLEN, MLA_ERR_BAD_TABLE, case_and_query, lse_of, status_of
+from oracle import cache as oc
+from test_gpu_cache import FMT, MLA_ERR_BAD_SEQLEN, MLA_ERR_BAD_TABLE, case_and_query, evict, lse_of, same, status_of, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +70,31 @@ def test_weights_leave_tokens_behind_a_bad_entry_alone(kv, B, G, page):
         assert torch.equal(got[0, at], start_weights(c.dims)[0, at])
         got[0, at] = good[0, at]
         assert torch.equal(got, good)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("mp,n,budget,bad", [(4, 250, 100, 0), (4, 250, 100, 1), (4, 250, 100, 3), (70, 4400, 1000, 9), (70, 4400, 1000, 40)])
+def test_evict_keeps_the_labels_of_rows_it_does_not_move(fmt, mp, n, budget, bad):
+    """Where an entry of a move is bad the row stays, and so must the weight
+    and the position that go with it."""
+    table, num_pages = tables(1, mp, mp)
+    S = mp * 64
+    g = torch.Generator().manual_seed(budget)
+    w, p = torch.rand(1, S, generator=g), torch.randperm(S, generator=g).int()[None]
+    lens = torch.tensor([n], dtype=torch.int32)
+    broken = table.clone()
+    broken[0, bad] = num_pages if bad % 2 else -3
+    raw, *got, st = evict(fmt, broken, num_pages, lens, w, p, budget, 10, 2)
+    assert st == MLA_ERR_BAD_TABLE
+    # the reference's moves, less those that touch the bad page
+    rows, want_n, want_w, want_p = oc.evict(raw, table, lens, w, p, budget, 10, 2)
+    moved_from = {int(x): i for i, x in enumerate(p[0, :n])}
+    skipped = 0
+    for to in range(budget):
+        src = moved_from[int(want_p[0, to])]
+        if src != to and bad in (to // 64, src // 64):
+            want_w[0, to], want_p[0, to] = w[0, to], p[0, to]
+            rows[int(table[0, to // 64]), to % 64] = raw[int(table[0, to // 64]), to % 64]
+            skipped += 1
+    assert skipped > 0
+    same(got, (rows, want_n, want_w, want_p))
