@@ -2,9 +2,11 @@
 // tensor-map encoding, kernel launches.  No allocation, no global state
 // beyond per-device launch-configuration caches and a cache of encoded
 // tensor maps.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <atomic>
+#include <limits>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -633,9 +635,14 @@ int mla_cache_weights(const mla_dims* d, int kv_format, const void* q_cat, const
   tl = tr;  // bf16 rows: latents and keys are columns of one view
   int sms = 0;
   if ((rc = sm_count(&sms)) != MLA_OK) return rc;
-  const DecodeArgs args = decode_args(d, q_cat, block_table, seq_lens, nullptr, nullptr,
-                                      static_cast<WsHeader*>(workspace), false, sms);
-  const float scale_lo = (float)((double)d->scale * 1.4426950408889634074 - (double)args.scale_log2);
+  DecodeArgs args = decode_args(d, q_cat, block_table, seq_lens, nullptr, nullptr, static_cast<WsHeader*>(workspace),
+                                false, sms);
+  // scale * log2 e in two parts, both above zero: a score of -infinity (a key
+  // that a row does not see) then stays one in the product with either
+  const double scale = (double)d->scale * 1.4426950408889634074;
+  args.scale_log2 = (float)scale;
+  if ((double)args.scale_log2 >= scale) args.scale_log2 = std::nextafter(args.scale_log2, 0.f);
+  const float scale_lo = std::max((float)(scale - (double)args.scale_log2), std::numeric_limits<float>::denorm_min());
   return cuda_status(launch_weights(kv_format, tl, tr, kv_cache, lse, weight, args, scale_lo,
                                     static_cast<cudaStream_t>(stream)));
 }

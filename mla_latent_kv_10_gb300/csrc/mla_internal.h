@@ -188,7 +188,8 @@ cudaError_t launch_evict(void* cache, int row_bytes, const int32_t* block_table,
 // The attention weights gathered by cached tokens (mla_weights.cu).  tm_lat
 // (bf16 cache only) and tm_rope: the rows' latents and RoPE keys in 64 x 64
 // boxes of bf16, 128-byte swizzle.  a: the fields of a decode that the split
-// and the scores need; scale_lo: what scale_log2 lacks to scale * log2 e.
+// and the scores need; scale_lo: what scale_log2 lacks to scale * log2 e
+// (both above zero).
 cudaError_t launch_weights(int kv_format, const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const void* cache,
                            const float* lse, float* weight, const DecodeArgs& a, float scale_lo, cudaStream_t st);
 cudaError_t launch_weights_fp8(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, const void* cache,

@@ -457,10 +457,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // ------------------------------------------------------------ summing warps
     const int r = 32 * warp + lane;  // token in the tile = TMEM lane
     const uint32_t lane_base = tmem + ((uint32_t)(32 * warp) << 16);
-    // score of a key that a row does not see: finite, as scale_lo may be
-    // negative (an infinity would meet its opposite), and far below any
-    // log-sum-exp once scaled
-    const float hidden = -fminf(0x1.fffffep127f, 0x1p100f / a.scale_log2);
+    // score of a key that a row does not see: weighs nothing at every scale, as
+    // both parts of the scale are above zero
+    constexpr float hidden = -INFINITY;
     uint32_t t = 0;
     while (next_range()) {
       const int n = walk.len(a, sb);
