@@ -516,9 +516,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
             for (int j = 0; j < 32; j += 4) {
               const float4 m = *reinterpret_cast<const float4*>(&sh.lse[c + j]);
               const float4 f = *reinterpret_cast<const float4*>(&sh.fix[c + j]);
+              // the small part last: added to the reference it would be
+              // rounded away (an exponent of hundreds has a half unit of 2^-16)
               auto weigh = [&](uint32_t x, float ref) {
                 const float y = __uint_as_float(x);
-                return ex2(fmaf(y, a.scale_log2, fmaf(y, scale_lo, -ref)));
+                return ex2(fmaf(y, scale_lo, fmaf(y, a.scale_log2, -ref)));
               };
               s4[0] = fmaf(weigh(v[j], m.x), f.x, s4[0]);
               s4[1] = fmaf(weigh(v[j + 1], m.y), f.y, s4[1]);
