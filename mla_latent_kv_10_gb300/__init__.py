@@ -227,8 +227,8 @@ def mla_project_uv(dims, o_lat, W_UV, out, stream=None):
 
 
 def mla_set_timeout_test(wait_limit_ns: int, stall_page: int):
-    """Testing hook of the decode kernel's timeout path (process-wide; 0, -1
-    restores the defaults)."""
+    """Testing hook of the timeout path of the decode and the gathered weights
+    (process-wide; 0, -1 restores the defaults)."""
     _check(load_library().mla_set_timeout_test(int(wait_limit_ns), int(stall_page)), "mla_set_timeout_test")
 
 

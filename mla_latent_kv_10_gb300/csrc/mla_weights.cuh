@@ -67,8 +67,9 @@ struct WCfg {
 //   rope_full, rope_empty   the same for the tile's RoPE keys (slot t % kRope)
 //   s_full, s_free[t & 1]   the scores are complete; they have been read
 //   q_full, q_free[p % kQBuf]  the pass's query is in shared memory; its products are done
+//   never                   testing: nothing completes it
 struct WShared {
-  uint64_t full[6], empty[6], rope_full[2], rope_empty[2], s_full[2], s_free[2], q_full[2], q_free[2], drain;
+  uint64_t full[6], empty[6], rope_full[2], rope_empty[2], s_full[2], s_free[2], q_full[2], q_free[2], drain, never;
   alignas(16) float lse[128];  // log2 units, rounded; +inf where a row adds nothing
   alignas(16) float fix[128];  // 2^-(what the rounding left off)
   int lrow[128];
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(bar(sh.q_free[s]), 1);
     }
     mbar_init(bar(sh.drain), 1);
+    mbar_init(bar(sh.never), 1);
     fence_mbar_init();
   }
   if (warp == kWMma) {
@@ -223,12 +225,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
     constexpr uint32_t id_l = kConvert ? idesc_f16(128, N, false, false) : idesc_bf16(128, N, false, false);
     constexpr uint32_t id_r = idesc_bf16(128, N, false, false);
     const uint32_t td = desc_lo(ring, 16), qd0 = desc_lo(qbase, 16), e = elect_one();
+    const uint32_t stall = a.stall_page >= 0 ? (uint32_t)a.stall_page / (kWTok / kPage) : 0xffffffffu;
     uint32_t x = 0, t = 0, p = 0;
     while (ok && next_range())
       for (int pass = 0; ok && pass < passes; ++pass, ++p) {
         const uint32_t qs = p % C::kQBuf, qd = qd0 + ((qs * C::kQBytes) >> 4);
         if (!(ok = wait(sh.q_full[qs], p / C::kQBuf))) break;
         for (int i = ta; ok && i < tb; ++i, ++t) {
+          if (t == stall && !(ok = wait(sh.never, 0))) break;
           if (t >= 2 && !(ok = wait(sh.s_free[t & 1], (t >> 1) - 1))) break;
           tc_fence_after();
           // two accumulators: the first half of the latent boxes, and the rest
