@@ -113,18 +113,28 @@ def _ptr(t):
     return None if t is None else t.data_ptr()  # an int: ctypes makes it a void*
 
 
-_raw_stream = None  # torch's (current device, its current stream) as integers, found on first use
+def _current_stream_of(torch):
+    """A function of no arguments: torch's current stream as an integer.  From
+    torch's own entry points where this torch has them (building its Stream
+    object costs about 4 us a call), otherwise by the public way."""
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if device is None or raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
+_current_stream = None  # found on first use
 
 
 def _stream(stream):
     if stream is None:
-        global _raw_stream
-        if _raw_stream is None:
+        global _current_stream
+        if _current_stream is None:
             import torch
             torch.cuda.current_stream()  # initialises CUDA
-            _raw_stream = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
-        device, raw = _raw_stream
-        return raw(device())
+            _current_stream = _current_stream_of(torch)
+        return _current_stream()
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
