@@ -799,17 +799,18 @@ __global__ void __launch_bounds__(Roles<kSolo, kFp8>::kThreads, 1)
     const int row = quad * 32 + lane;  // TMEM lane = query row in this block
     // this CTA's rows: every (l, h) in pair mode; in solo mode (l, h) for
     // the heads h of its latent half, l-major
-    const int lrow = (int)rg * kRowsPerCta + row;    // index in this CTA's list
     int l, h, grow;
     bool valid;
     if constexpr (kSolo) {
       const int hh = a.H / 2;                        // heads per l in this CTA's list
-      valid = lrow < a.Lq * hh;
+      const int block = kRowsPerCta / hh * hh;       // rows of a block: whole tokens (see decode_csize)
+      const int lrow = (int)rg * block + row;        // index in this CTA's list
+      valid = row < block && lrow < a.Lq * hh;
       l = valid ? lrow / hh : 0;
       h = valid ? (int)r * hh + lrow % hh : 0;
       grow = l * a.H + h;                            // row of the (l, h) list of all heads
     } else {
-      grow = lrow;
+      grow = (int)rg * kRowsPerCta + row;
       valid = grow < a.rows;
       l = valid ? grow / a.H : 0;
       h = valid ? grow % a.H : 0;
@@ -840,19 +841,21 @@ __global__ void __launch_bounds__(Roles<kSolo, kFp8>::kThreads, 1)
     auto load_q = [&](int b) {
       if (!ok) return;
       if (leader) {
-        mbar_arrive_expect_tx(bar(sh.q_tma), L::kQRopeBytes);
         if constexpr (kSolo) {
           // all 64 RoPE columns, one run of hh rows (the CTA's heads of one
           // token l) per box; runs past the last token read the next
-          // sequence's rows or the zero fill, which nobody uses
-          const int hh = a.H / 2;
-          for (int run = 0; run < kRowsPerCta / hh; ++run) {
-            const int lr = ((int)rg * kRowsPerCta) / hh + run;
+          // sequence's rows or the zero fill, which nobody uses, and rows
+          // behind the last run (hh does not divide 128) hold whatever was there
+          const int hh = a.H / 2, runs = kRowsPerCta / hh;
+          mbar_arrive_expect_tx(bar(sh.q_tma), L::kRopeBoxes * runs * hh * 64);
+          for (int run = 0; run < runs; ++run) {
+            const int lr = (int)rg * runs + run;
             for (int j = 0; j < 2; ++j)
               tma_load_2d(qrope + j * kQRopeBox + run * hh * 64, &tm_qrope, bar(sh.q_tma), a.d_g + 32 * j,
                           (b * a.Lq + lr) * a.H + (int)r * hh);
           }
         } else {
+          mbar_arrive_expect_tx(bar(sh.q_tma), L::kQRopeBytes);
           tma_load_2d(qrope, &tm_qrope, bar(sh.q_tma), a.d_g + 32 * (int)r, b * a.Lq * a.H + (int)rg * kRowsPerCta);
         }
         ++nq_tma;

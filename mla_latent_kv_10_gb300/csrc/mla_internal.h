@@ -219,13 +219,16 @@ cudaError_t launch_prefill_attend(const CUtensorMap& tmQN, const CUtensorMap& tm
                                   const int32_t* seq_lens, void* out, float* lse, WsHeader* ws, int B, int Lq,
                                   int H, int max_pages, int num_pages, float scale, unsigned long long wait_ns,
                                   cudaStream_t st);
-// CTAs per cluster of the decode launch: a pair per 128 query rows of a
-// sequence (in solo mode each CTA of the pair holds half the heads)
+// CTAs per cluster of the decode launch: a pair per block of up to 128 query
+// rows of a sequence (in solo mode each CTA of the pair holds half the heads,
+// and a block takes whole new tokens, as the heads of one token are copied by
+// one box: 128 / (H / 2) of them)
 inline bool decode_solo(int G) { return G > 1; }
 inline int decode_plan_max_b(int G) { return decode_solo(G) ? kPlanInKernelMaxBSolo : kPlanInKernelMaxB; }
 inline int decode_csize(int Lq, int H, int G) {
-  const int rows_per_cta = decode_solo(G) ? Lq * (H / 2) : Lq * H;
-  return 2 * ((rows_per_cta + kRowsPerCta - 1) / kRowsPerCta);
+  const int per = decode_solo(G) ? kRowsPerCta / (H / 2) * (H / 2) : kRowsPerCta;
+  const int rows = decode_solo(G) ? Lq * (H / 2) : Lq * H;
+  return 2 * ((rows + per - 1) / per);
 }
 
 }  // namespace mla
