@@ -39,8 +39,8 @@
  *     workspace; read it with mla_get_device_status.
  *   - Nothing is thrown across the ABI.  Every call is thread-safe as long as
  *     concurrent calls do not share output buffers or workspaces.
- *   - mla_absorb_q, mla_decode_paged and mla_project_uv launch their kernels
- *     with programmatic dependent launch: a kernel may start its on-chip
+ *   - mla_absorb_q, the mla_decode_paged* calls, mla_project_uv and the
+ *     mla_cache_* calls launch their kernels with programmatic dependent launch: a kernel may start its on-chip
  *     set-up while the kernel before it on the stream is still running, but
  *     reads and writes global memory only after that kernel has completed.
  *     Stream order therefore holds for every caller kernel in between, as
@@ -450,7 +450,11 @@ int mla_prefill_attend(const mla_dims* dims, const void* q_nope, const void* q_r
  *   FP4: scale e4m3(min(amax / 6, 448)) per 16 columns; codes
  *        e2m1(clamp(x / scale, +-6)), 0 where the scale is 0
  * both rounded to nearest, ties to even.  A block that holds an infinity or a
- * NaN reads back as NaN and sets MLA_ERR_RANGE.
+ * NaN reads back as NaN and sets MLA_ERR_RANGE.  An FP4 block whose greatest
+ * value is at most 6 * 2^-10 (0.0059) has scale 0 and is stored as zeros, one
+ * below 6 * 2^-6 (0.094) a subnormal scale of fewer than four significant
+ * bits: latents that small are multiplied by a power of two before they are
+ * appended, and W_UK and W_UV divided by it (see mla_decode_paged_fp4).
  * position (may be NULL): receives start_position[b] + l of each written
  *   token (start_position int32 [B]; NULL: its cached place, which is its
  *   text position only while nothing of the sequence has been evicted: an
