@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(kThreads, kCombineThreads / kThreads)
             *reinterpret_cast<const uint4*>(&tile[rr][pc * 8]);
     }
   };
-  if constexpr (kColsMax < kCombineCols) {
+  // (256 and 512 columns gain from the finer split with few partials too, and
+  // the branch would cost them 0.2 us with many)
+  if constexpr (kColsMax < kCombineCols && DG <= 2 * kFineCols) {
     if (nseg <= kShortSeg) {
       merge_short<DG, kCols>(o_part, lse_part, tile, lse_out ? lse_out + (size_t)b * rows : nullptr, rows, r0, cz, H, G,
                              seg0, nseg);
