@@ -18,12 +18,12 @@
 //   * bf16 cache: boxes by TMA.  FP8, FP4: eight warps convert codes * scale
 //     to f16 (exact, see the decodes); the RoPE keys come by TMA in bf16.
 //   * warps 0-3 sum, 4-11 load (query, conversion), 12 issues MMAs, 13 copies.
-// 16 sequences of 4096 tokens, 128 heads, FP4: 19.8 us (21.6 with all eight
+// 16 sequences of 4096 tokens, 128 heads, FP4: 20.0 us (1.8 more with all eight
 // converting warps on one box at a time).  Of 35,000 cycles 10,500 stage the
 // query (147 KB a CTA, 22 MB over all of them, from L2), then each of four tiles
 // takes 5,000, bound by the way of a box from its conversion over the products
-// to a free place in a ring of three.  Over long bf16 sequences it reads at 0.54
-// of the memory's rate (5 of 777 to 30011 tokens, 3 x 64 rows, 4 groups: 29 us).
+// to a free place in a ring of three.  Over long bf16 sequences it reads at 0.53
+// of the memory's rate (5 of 777 to 30011 tokens, 3 x 64 rows, 4 groups: 29.7 us).
 #pragma once
 #include <cmath>
 
