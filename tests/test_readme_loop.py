@@ -1,6 +1,6 @@
-"""The serving loop that README.md prints, run as it stands: after every step
-the cache holds the newest and the first text positions of each sequence.  On
-the CPU against the reference's calls, on the GPU against the library's."""
+"""The serving loop that the front page prints, run as it stands: after every
+step the cache holds the newest and the first text positions of each sequence.
+On the CPU against the reference's calls, on the GPU against the library's."""
 import os
 import re
 import types
